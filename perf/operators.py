@@ -409,9 +409,9 @@ def run(st):
 
 def _own_append(st):
     cache, stream = st["cache"], torch.cuda.current_stream()
-    streams = st["case"]["B"]
-    for i, (k, v) in enumerate(zip(st["k"].flatten(0, 1).unbind(), st["v"].flatten(0, 1).unbind())):
-        cache.append_frame(i % streams, i // streams, k, v, stream)
+    for b in range(st["case"]["L"]):
+        for s in range(st["case"]["B"]):
+            cache.append_frame(s, b, st["k"][b, s], st["v"][b, s], stream)
     for s in range(st["case"]["B"]):
         cache.rollback_frame(s)
     return st["views"]
@@ -433,8 +433,8 @@ def _own_weigh(st):
 
 def _own_evict(st):
     cache, c, stream = st["cache"], st["case"], torch.cuda.current_stream()
-    for b, (k, v) in enumerate(zip(st["k"].unbind(), st["v"].unbind())):
-        cache.append_frame(0, b, k, v, stream)
+    for b in range(c["L"]):
+        cache.append_frame(0, b, st["k"][b], st["v"][b], stream)
     cache.evict_frames(0)
     cache.evict_specials(0, c["keep"], c["recent"], st["ws"], stream)
     return _evict_outputs(st)
