@@ -318,7 +318,9 @@ int spk_track_specials(spk_cache* cache, float* weights, int32_t* ids, void* cud
  * not depend on the order of execution: two equal calls add the same bits.  Requires tracking
  * (spk_track_specials), a current plan and the block appended, like spk_run_attention.  Calls that
  * are given one workspace use the same scratch: their GPU work runs in order (one stream, or
- * streams ordered by events), this one's and the attention calls' alike. */
+ * streams ordered by events), this one's and the attention calls' alike.  While the workspace
+ * reports a device-side wait that gave up (spk_read_device_status reads and clears the report),
+ * in this call or before it, nothing is added. */
 int spk_accumulate_weights(spk_cache* cache, int block, const void* q, const float* lse, void* workspace,
                            void* cuda_stream);
 

@@ -124,13 +124,15 @@ __global__ void __launch_bounds__(kWThreads) weight_f32_kernel(const WeightParam
   }
 }
 
-// weights[s][j] += sum over heads, in head order
+// weights[s][j] += sum over heads, in head order.  Nothing is added where a wait of this call (or of
+// an earlier one whose report has not been read) gave up: `part` is then incomplete, and the weights
+// are a running total that could not be put right again.
 __global__ void __launch_bounds__(256) weight_sum_kernel(const WeightParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int stream = blockIdx.y;
   const int j = blockIdx.x * 256 + threadIdx.x;
-  if (j >= p.streams[stream].specials) return;
+  if (j >= p.streams[stream].specials || *p.status == kStatusWaitTimeout) return;
   const float* src = p.part + int64_t(stream) * p.H * p.cap + j;
   float sum = 0.f;
   for (int h = 0; h < p.H; ++h) sum += src[int64_t(h) * p.cap];
