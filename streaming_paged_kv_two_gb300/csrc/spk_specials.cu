@@ -74,11 +74,10 @@ __global__ void __launch_bounds__(kWThreads) weight_f32_kernel(const WeightParam
     __syncthreads();
     for (int i = tid; i < kWRows * (D / 4); i += kWThreads) {
       const int r = i / (D / 4), d = 4 * (i % (D / 4));
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (r0 + r < p.T) {
-        const int64_t at = ((int64_t(stream) * p.T + r0 + r) * p.H + head) * D + d;
-        v = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + at));
-      }
+      // (past the last row: that row again, with an lse of +inf.  Zeros would turn an infinite key's
+      // score into a NaN that no row has.)
+      const int64_t at = ((int64_t(stream) * p.T + min(r0 + r, p.T - 1)) * p.H + head) * D + d;
+      const float4 v = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + at));
       *reinterpret_cast<float4*>(Qs + r * C::kLd + d) = v;
     }
     if (tid < kWRows)  // rows past the last get +inf: weight 0

@@ -189,8 +189,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = threadIdx.x; i < padded * (D / 8); i += kThreads) {
       const int r = i / (D / 8), c = i % (D / 8);
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (r < p.rows) v = __ldg(reinterpret_cast<const uint4*>(q0 + r * q_stride) + c);
+      // (past the last row: that row again, at weight 0 below.  Zeros would turn an infinite key's
+      // score into a NaN that no row has.)
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(q0 + min(r, p.rows - 1) * q_stride) + c);
       if constexpr (kE4m3) {
         const uint32_t x0[2] = {v.x, v.y}, x1[2] = {v.z, v.w};
         uint32_t hi[2], lo[2];

@@ -63,3 +63,49 @@ def test_a_reported_timeout_adds_nothing(kind):
     assert float(h.weights[:, :n].min()) > 0.5
     assert h.status() == 0
     h.close()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("rows", [1, 6, 206, 402])
+def test_keys_of_minus_infinite_score_weigh_nothing(kind, D, rows):
+    """A special key with an infinite element that every query row meets with the other sign: its
+    scores are -inf, its weight is 0 (and it is the first to leave), whatever rows the last tile lacks."""
+    from budget_harness import to_device
+    w = work(frames=8, head_dim=D)
+    h = harness(w, kind, max_query_frames=2)
+    P = w.patches_per_frame
+
+    def kv(f):
+        def rows_of(s, b):
+            k, v = wl.frame_kv(w, s, b, f)
+            k = wl.bf16_bits_to_f32(k)
+            if f == 3:
+                k[P + 2, :, 5] = np.inf
+            return (wl.f32_to_bf16_bits(k), v) if kind == "bf16" else (k, wl.bf16_bits_to_f32(v))
+        return rows_of
+
+    h.track()
+    for f in range(w.frames):
+        h.append(f, kv(f))
+    q = wl.to_f64(h.queries(rows, 4), h.w.dtype).astype(np.float32)
+    q[:, :, 5] = -np.abs(q[:, :, 5]) - np.float32(0.25)
+    q = wl.f32_to_bf16_bits(q) if kind == "bf16" else q
+    k, v = h.visible(0, 0)
+    with np.errstate(invalid="ignore"):
+        _, lse = oracle.attend(wl.to_f64(q, h.w.dtype), k, v)
+    assert np.isfinite(lse).all()
+    h.cache.plan_rows(rows, h.ws, h.st)
+    h.cache.accumulate_weights(0, to_device(q, h.w.dtype), torch.from_numpy(lse.astype(np.float32)).cuda(), h.ws, h.st)
+    torch.cuda.synchronize()
+    n = w.frames * w.specials_per_frame
+    got = h.weights[0, :n].cpu().numpy()
+    dead = 3 * w.specials_per_frame + 2
+    assert got[dead] == 0 and np.isfinite(got).all()
+    exact = oracle.key_weights(wl.to_f64(q, h.w.dtype), np.stack([r[0] for r in h.special[(0, 0)]]), lse)
+    # a score of at most 20 in fp32 (its D roundings, the log-sum-exp's and the exponential's)
+    live = np.arange(n) != dead
+    assert np.abs(got[live] / exact[live] - 1).max() <= (2 * D + 64) * 2.0 ** -24 * 20
+    assert h.evict(0, n - 1, 0)[dead] == n - 1
+    assert h.status() == 0
+    h.close()
