@@ -331,7 +331,8 @@ int spk_accumulate_weights(spk_cache* cache, int block, const void* q, const flo
  * positions >= keep move, in ascending order, into the vacated positions < keep, in ascending
  * order, with their K/V (and scales) in every block's pool, weight and id; no other slot is
  * written.  Special pages past the last survivor return to the front of the free list.
- * The choice is made on the device: the call does not synchronise.  workspace: as for spk_plan,
+ * The choice is made on the device, and the page list travels in launch parameters: the call does not
+ * wait for the GPU.  workspace: as for spk_plan,
  * with its GPU work in order as above; not on a stream that is being captured
  * (SPK_ERR_BAD_STATE: the page list is the host's of the moment).
  * Marks the plan stale when tokens leave.

@@ -411,48 +411,27 @@ int build_plan(spk_cache* c) {
   return SPK_OK;
 }
 
-// The next of the two pinned staging buffers, free of earlier copies.
-int next_staging(spk_cache* c, int* index) {
-  const int i = c->stage_idx;
-  c->stage_idx ^= 1;
-  if (c->staged_used[i]) {
-    cudaError_t e = cudaEventSynchronize(c->staged[i]);
-    if (e != cudaSuccess) return cuda_fail(e, "staging wait");
-  }
-  *index = i;
-  return SPK_OK;
-}
-
-// Copy `bytes` of a staging buffer to the device.
-int send_staging(spk_cache* c, int i, void* dst, size_t bytes, cudaStream_t stream) {
-  cudaError_t e = cudaMemcpyAsync(dst, c->staging[i], bytes, cudaMemcpyHostToDevice, stream);
-  if (e != cudaSuccess) return cuda_fail(e, "table upload");
-  e = cudaEventRecord(c->staged[i], stream);
-  if (e != cudaSuccess) return cuda_fail(e, "staging event");
-  c->staged_used[i] = true;
-  return SPK_OK;
-}
-
-// A host array to the device through the staging buffers (which hold the plan's tables, so
-// any list of one entry per page fits).
-int upload(spk_cache* c, const void* src, size_t bytes, void* dst, cudaStream_t stream) {
-  int i = 0, rc = next_staging(c, &i);
-  if (rc) return rc;
-  std::memcpy(c->staging[i], src, bytes);
-  return send_staging(c, i, dst, bytes, stream);
-}
-
 int upload_plan(spk_cache* c, void* workspace, cudaStream_t stream) {
   const WorkspaceLayout& L = c->ws;
-  int i = 0, rc = next_staging(c, &i);
-  if (rc) return rc;
+  const int i = c->stage_idx;
+  c->stage_idx ^= 1;
+  cudaError_t e;
+  if (c->staged_used[i]) {
+    e = cudaEventSynchronize(c->staged[i]);
+    if (e != cudaSuccess) return cuda_fail(e, "plan staging wait");
+  }
   char* h = c->staging[i];
   const size_t base = L.streams;
   std::memcpy(h + (L.streams - base), c->sdesc.data(), sizeof(StreamDesc) * c->sdesc.size());
   std::memcpy(h + (L.chunks - base), c->chunks.data(), sizeof(ChunkDesc) * c->chunks.size());
   std::memcpy(h + (L.works - base), c->works.data(), sizeof(WorkDesc) * c->works.size());
   const size_t bytes = L.works - base + sizeof(WorkDesc) * c->works.size();
-  return send_staging(c, i, static_cast<char*>(workspace) + base, bytes, stream);
+  e = cudaMemcpyAsync(static_cast<char*>(workspace) + base, h, bytes, cudaMemcpyHostToDevice, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "plan upload");
+  e = cudaEventRecord(c->staged[i], stream);
+  if (e != cudaSuccess) return cuda_fail(e, "plan staging event");
+  c->staged_used[i] = true;
+  return SPK_OK;
 }
 
 }  // namespace
@@ -1048,19 +1027,24 @@ int spk_evict_specials(spk_cache* c, int stream, int64_t keep, int recent_frames
       return fail(SPK_ERR_BAD_STATE, "an eviction cannot be captured: its page list is the host's of the moment");
     char* ws = static_cast<char*>(workspace);
     int32_t* pages = reinterpret_cast<int32_t*>(ws + c->ws.evict);
-    if ((rc = upload(c, s.special_pages.data(), sizeof(int32_t) * s.special_pages.size(), pages, st))) return rc;
+    PageListParams list;
+    for (size_t i = 0; i < s.special_pages.size(); i += kListPages) {
+      list.dst = pages + i;
+      list.count = int32_t(std::min<size_t>(kListPages, s.special_pages.size() - i));
+      std::copy_n(s.special_pages.begin() + i, list.count, list.pages);
+      err = launch_page_list(list, st);
+      if (err != cudaSuccess) return cuda_fail(err, "page list kernel launch");
+    }
     EvictParams e{};
     const int64_t at = int64_t(stream) * c->ws.special_cap;
     e.weights = c->weights + at;
     e.ids = c->ids + at;
-    e.pages = pages;
     e.count = pages + g.max_special_pages;
     e.holes = e.count + 64;
     e.sources = e.holes + c->ws.special_cap;
     e.n = n;
     e.keep = keep;
     e.first_recent_id = int32_t((s.frame_count - std::min<int64_t>(recent_frames, s.frame_count)) * g.specials_per_frame);
-    e.ps = g.page_size;
     err = launch_evict_select(e, st);
     if (err != cudaSuccess) return cuda_fail(err, "selection kernel launch");
     for (int b0 = 0; b0 < g.num_blocks; b0 += kMovePools) {

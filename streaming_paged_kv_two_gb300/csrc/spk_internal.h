@@ -146,18 +146,24 @@ struct WeightParams {
   long long wait_limit_ns;
 };
 
+// Page ids that one launch carries to the device in its parameters (longer lists take several).
+constexpr int kListPages = 1000;
+struct PageListParams {
+  int32_t* dst;
+  int32_t count;
+  int32_t pages[kListPages];
+};
+
 // Pools of one move launch (larger models take several launches).
 constexpr int kMovePools = 128;
 struct EvictParams {
   float* weights;             // this stream's records
   int32_t* ids;
-  const int32_t* pages;       // the stream's special pages in order
   int32_t* count;             // moves chosen
   int32_t* holes;             // positions < keep that leave, ascending
   int32_t* sources;           // survivors at positions >= keep, ascending
   int64_t n, keep;
   int32_t first_recent_id;    // tokens with an id at or past this (modulo 2^32) are kept
-  int32_t ps;
 };
 struct MoveParams {
   char* pools[kMovePools];
@@ -262,6 +268,7 @@ cudaError_t launch_weights_tc(const WeightParams& p, const CUtensorMap* map, boo
 // Once per cache, with its device current: dynamic shared memory of the weight kernels.
 cudaError_t configure_weights_tc();
 cudaError_t configure_weights_f32();
+cudaError_t launch_page_list(const PageListParams& p, cudaStream_t s);
 cudaError_t launch_evict_select(const EvictParams& p, cudaStream_t s);
 cudaError_t launch_evict_move(const MoveParams& p, cudaStream_t s);
 cudaError_t launch_attention_bf16(const AttnParams& p, const CUtensorMap* kv_map, cudaStream_t s);

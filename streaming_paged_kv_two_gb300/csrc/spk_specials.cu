@@ -287,6 +287,16 @@ __global__ void __cluster_dims__(kCtas) __launch_bounds__(kSelThreads) evict_sel
   cluster.sync();  // no CTA leaves while another reads its memory
 }
 
+// ------------------------------------------------------------------ eviction: the page list
+// The stream's special pages in order, by way of the launch's parameters: a copy from pinned memory
+// would make a host that evicts several streams a frame wait for a staging buffer until the frame's
+// GPU work is done.
+__global__ void __launch_bounds__(256) page_list_kernel(const __grid_constant__ PageListParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  for (int i = threadIdx.x; i < p.count; i += blockDim.x) p.dst[i] = p.pages[i];
+}
+
 // ------------------------------------------------------------------ eviction: the moves
 // Survivor sources[i] into holes[i], K and V (and scale bytes) of every pool of the launch.
 // Sources lie at or past `keep`, holes below it: no move reads what another writes.  As many CTAs as
@@ -347,6 +357,10 @@ cudaError_t launch_weights(const WeightParams& p, int dtype, const CUtensorMap* 
   if (e != cudaSuccess) return e;
   return launch_dependent(weight_sum_kernel, dim3(unsigned((p.max_specials + 255) / 256), unsigned(p.B)), dim3(256), 0,
                           s, p);
+}
+
+cudaError_t launch_page_list(const PageListParams& p, cudaStream_t s) {
+  return launch_dependent(page_list_kernel, dim3(1), dim3(256), 0, s, p);
 }
 
 cudaError_t launch_evict_select(const EvictParams& p, cudaStream_t s) {

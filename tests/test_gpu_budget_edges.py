@@ -109,3 +109,47 @@ def test_keys_of_minus_infinite_score_weigh_nothing(kind, D, rows):
     assert h.evict(0, n - 1, 0)[dead] == n - 1
     assert h.status() == 0
     h.close()
+
+
+# ---------------------------------------------------------------- eviction
+
+def test_evictions_of_many_streams_do_not_wait_for_the_gpu():
+    """One plan and five evictions, twice over, queued behind a kernel that runs for a good while:
+    the calls return before it has ended, and give what they give on an idle GPU."""
+    w = work(num_streams=5, frames=4, patches_per_frame=8, page_size=16)
+    h = harness(w, "e4m3")
+    h.track()
+    for f in range(w.frames):
+        h.append(f)
+    n = w.frames * w.specials_per_frame
+    h.weights[:, :n] = torch.arange(n, device="cuda", dtype=torch.float32)
+    torch.cuda.synchronize()
+    for keep in (20, 15):
+        done = torch.cuda.Event()
+        torch.cuda._sleep(1_000_000_000)
+        done.record()
+        h.cache.plan(h.ws, h.st)
+        for s in range(w.num_streams):
+            h.cache.evict_specials(s, keep, 0, h.ws, h.st)
+        assert not done.query()
+        torch.cuda.synchronize()
+        # the lowest positions have the least weight: the newest tokens are left
+        assert [sorted(x) for x in h.ids[:, :keep].tolist()] == [list(range(n - keep, n))] * w.num_streams
+    h.close()
+
+
+def test_eviction_over_more_pages_than_one_launch_lists():
+    from test_gpu_budget import check_pool
+    w = work(num_blocks=2, num_heads=1, frames=1100, specials_per_frame=4, patches_per_frame=2, page_size=4)
+    h = harness(w, "e4m3")
+    h.track()
+    for f in range(w.frames):
+        h.append(f)
+    n = w.frames * w.specials_per_frame
+    g = np.random.default_rng(2)
+    for keep in (4100, 4001, 90):
+        n = len(h.special[(0, 0)])
+        h.weights[0, :n] = torch.from_numpy(g.random(n).astype(np.float32)).cuda()
+        h.evict(0, keep, 3)
+        check_pool(h, 0, keep)
+    h.close()
