@@ -100,9 +100,12 @@ typedef struct {
   int32_t max_patch_pages;     /* MPP per stream, >= 1 (the pages' sizing: sc + w + 16) */
   int32_t max_special_pages;   /* MSP per stream, >= 1 (ceil(max_total_frames * S / ps)) */
   int32_t dtype;               /* enum spk_dtype */
-  int32_t splits_per_stream;   /* 0 = planner's choice; k > 0 forces k KV splits per stream (clamped to [1, chunks]) */
+  int32_t splits_per_stream;   /* 0 = planner's choice; k > 0 forces k KV splits per stream (clamped to [1, chunks], to 32 and,
+                                  for SPK_E4M3, to 256 while the plan's rows allow it: see max_query_frames) */
   int32_t max_query_frames;    /* most frames of queries one attention call may carry (spk_plan_queries);
-                                  0 or 1 = one frame per call.  Sizes the workspace's split partials. */
+                                  0 or 1 = one frame per call.  Sizes the workspace's split partials: 32 splits of that many
+                                  frames' rows, SPK_E4M3 also up to 256 (fewer with many heads and streams) of one
+                                  frame's.  Plans of SPK_E4M3 caches take as many splits as fit. */
   const int32_t* patch_page_order;   /* optional host array [B*MPP]: initial free-list order, global ids;
                                         entries [s*MPP, (s+1)*MPP) must permute stream s's patch ids. NULL = ascending */
   const int32_t* special_page_order; /* optional host array [B*MSP], same rule for special ids. NULL = ascending */

@@ -598,7 +598,7 @@ cudaError_t configure_rows() {
 // of 16 heads of 64 dims: 1 row 47 / 78, 16 rows 53 / 90, 32 rows 84 / 92, 48 rows 119 / 92; over 4 x
 // 63,792 keys of 8 heads of 128 dims: 16 rows 121 / 205, 32 rows 202 / 207, 48 rows 287 / 209.  Up to 8
 // rows the tile of 8 takes 47 where that of 16 takes 53 (D = 128: 107 and 119).
-constexpr int kRowsOne = 8, kRowsMost = 32;
+constexpr int kRowsOne = 8, kRowsMost = kE4m3RowsMost;
 
 cudaError_t configure_attention_e4m3() {
   for (const cudaError_t e : {configure_rows<64, 8>(), configure_rows<64, 16>(), configure_rows<128, 8>(),

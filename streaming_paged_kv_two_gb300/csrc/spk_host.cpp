@@ -147,12 +147,22 @@ WorkspaceLayout make_layout(const spk_config& c) {
   L.works = off;   off = align256(off + sizeof(WorkDesc) * L.max_splits);
   L.plan_end = off;
   const int64_t Tq = T * std::max(1, c.max_query_frames);  // query rows per stream of the largest plan
-  L.part_o = off;  off = align256(off + sizeof(float) * size_t(L.max_splits) * c.num_heads * Tq * c.head_dim);
-  L.part_lse = off; off = align256(off + sizeof(float) * size_t(L.max_splits) * c.num_heads * Tq);
-  L.part_w = off;  off = align256(off + sizeof(float) * size_t(B) * c.num_heads * size_t(L.special_cap));
-  // page list, move count, holes, sources
-  L.evict = off;
-  off = align256(off + sizeof(int32_t) * (size_t(c.max_special_pages) + 64 + 2 * size_t(L.special_cap)));
+  // Split partials.  More splits than kMaxSplitsPerStream serve calls of few rows (one frame's, or
+  // those of the rows kernel), so rows times splits is what is bounded (split_limit).
+  L.part_rows = kMaxSplitsPerStream * Tq;
+  if (c.dtype == SPK_E4M3)
+    L.part_rows = std::max(L.part_rows, L.max_splits_per_stream * std::min(Tq, std::max<int64_t>(T, kE4m3RowsMost)));
+  const size_t rows = size_t(B) * size_t(L.part_rows) * c.num_heads;
+  L.part_o = off;
+  L.part_lse = align256(L.part_o + sizeof(float) * rows * c.head_dim);
+  // An accumulation's and an eviction's scratch lies over the partials: a call's GPU work has ended
+  // with the partials before the next one given this workspace begins.
+  L.part_w = L.part_o;
+  L.evict = L.part_o;  // page list, move count, holes, sources
+  off = std::max({L.part_lse + sizeof(float) * rows,
+                  L.part_w + sizeof(float) * size_t(B) * c.num_heads * size_t(L.special_cap),
+                  L.evict + sizeof(int32_t) * (size_t(c.max_special_pages) + 64 + 2 * size_t(L.special_cap))});
+  off = align256(off);
   L.total = off;
   return L;
 }
@@ -293,6 +303,11 @@ int allocate_frame(spk_cache* c, StreamState& s) {
   return SPK_OK;
 }
 
+// Most KV splits per stream of a plan of c->Tq query rows: what the workspace's partials hold.
+int split_limit(const spk_cache* c) {
+  return int(std::min<int64_t>(c->ws.max_splits_per_stream, c->ws.part_rows / c->Tq));
+}
+
 // KV splits per stream.  bf16: one CTA per SM and per (split, head, row group);
 // pick n minimising waves * (chunks per split + per-CTA overhead) + a small
 // charge per split for the partials it writes and the merge reads back.
@@ -302,7 +317,7 @@ int choose_splits(const spk_cache* c, const std::vector<int32_t>& nchunks, std::
   nsplit.assign(B, 1);
   if (g.splits_per_stream > 0) {
     for (int s = 0; s < B; ++s)
-      nsplit[s] = std::max(1, std::min({g.splits_per_stream, nchunks[s], int(c->ws.max_splits_per_stream)}));
+      nsplit[s] = std::max(1, std::min({g.splits_per_stream, nchunks[s], split_limit(c)}));
     return SPK_OK;
   }
   int32_t cmax = 0;
@@ -323,7 +338,7 @@ int choose_splits(const spk_cache* c, const std::vector<int32_t>& nchunks, std::
   const double merge_charge = g.dtype == SPK_E4M3 ? e4m3_merge_charge(c->Tq) : 0.0;
   int best = 1;
   double best_cost = 1e300;
-  for (int n = 1; n <= std::min<int>(int(c->ws.max_splits_per_stream), std::max(1, cmax)); ++n) {
+  for (int n = 1; n <= std::min(split_limit(c), std::max(1, cmax)); ++n) {
     const double waves = std::ceil(double(per_split_ctas) * n / slots);
     const double cost =
         waves * (std::ceil(double(cmax) / n) + overhead_chunks) + split_charge * n + (n > 1 ? merge_charge : 0.0);

@@ -20,6 +20,8 @@ constexpr int kMaxSplitsPerStream = 32;
 // (kE4m3Ctas in all), so that a call with one query row still draws on the whole memory system.
 constexpr int kE4m3Ctas = 608;
 constexpr int kMaxSplitsE4m3 = 256;
+// Query rows up to which the rows kernel serves a call (see launch_attention_e4m3).
+constexpr int kE4m3RowsMost = 32;
 // Scale bytes of one (page, K/V, head) of an SPK_E4M3 pool: page_size rounded up to this, so a
 // chunk's 128 bytes are one aligned run.
 constexpr int kScaleRow = 128;
@@ -70,14 +72,15 @@ struct WorkspaceLayout {
   size_t chunks = 0;     // ChunkDesc[max_chunks]
   size_t works = 0;      // WorkDesc[max_splits]
   size_t plan_end = 0;   // end of the part uploaded by plan
-  size_t part_o = 0;     // float[max_splits][H][D/4][T][4] (see part_o_offset)
-  size_t part_lse = 0;   // float[max_splits][H][T]  (log2 units)
+  size_t part_o = 0;     // float[splits][H][D/4][T][4] (see part_o_offset): part_rows splits x rows a stream
+  size_t part_lse = 0;   // float[splits][H][T]  (log2 units)
   size_t part_w = 0;     // float[B][H][special_cap]: per-head key weights of one accumulate call
-  size_t evict = 0;      // int32 pages[max_special_pages], EvictScratch, int32 holes[cap], sources[cap]
+  size_t evict = 0;      // int32 pages[max_special_pages], count[64], holes[cap], sources[cap]
   size_t total = 0;
   int64_t max_chunks = 0;
   int64_t max_splits = 0;
   int64_t max_splits_per_stream = 0;
+  int64_t part_rows = 0;    // splits x query rows of a stream that the partials hold
   int64_t special_cap = 0;  // special tokens per stream: max_special_pages * page_size
 };
 

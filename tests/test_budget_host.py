@@ -82,6 +82,39 @@ def test_workspace_covers_one_row_over_many_splits():
     assert small >= 256 * 13 * 64 * 4     # 256 splits of one head
 
 
+def test_workspace_of_many_query_frames_is_not_sized_for_many_splits():
+    """Up to 256 splits serve calls of few rows: the partials of 64 frames' rows are those of 32 splits."""
+    frames = dict(num_heads=1, patches_per_frame=256, specials_per_frame=6, page_size=256, max_query_frames=64)
+    e4m3, bf16 = (spk.required_bytes(make(t, **frames)[0])[1] for t in (spk.SPK_E4M3, spk.SPK_BF16))
+    assert e4m3 <= bf16 + (1 << 20)
+    frames.update(num_heads=4, head_dim=128, patches_per_frame=999, page_size=1024)
+    e4m3, bf16 = (spk.required_bytes(make(t, **frames)[0])[1] for t in (spk.SPK_E4M3, spk.SPK_BF16))
+    assert e4m3 <= bf16 + (1 << 20)
+
+
+@pytest.mark.parametrize("dtype", [spk.SPK_E4M3, spk.SPK_BF16, spk.SPK_F32])
+def test_workspace_holds_no_scratch_of_its_own_for_the_budget(dtype):
+    """A longer special stream adds plan tables (8 bytes a chunk); its weights' and evictions' scratch
+    (4 bytes a head and 8 a token) lies over the partials."""
+    size = dict(num_heads=16, patches_per_frame=256, specials_per_frame=6, page_size=256)
+    short, long = (spk.required_bytes(make(dtype, max_special_pages=n, **size)[0])[1] for n in (1, 235))
+    assert long - short <= 234 * 8 * (4 if dtype == spk.SPK_E4M3 else 2) + 512
+
+
+def test_splits_follow_the_planned_rows():
+    """200 forced splits: every chunk of 3 patch and 188 special pages for a row and for a frame, as many
+    as the partials hold (10,240 rows) for two and for eight."""
+    cfg, _ = make(num_heads=1, patches_per_frame=30, specials_per_frame=10, page_size=64, max_special_pages=200,
+                  splits_per_stream=200, max_query_frames=8)
+    c = spk.Cache(cfg)
+    for _ in range(1200):
+        c.append_frame(0, 0)
+        c.evict_frames(0)
+    for rows, splits in ((1, 191), (40, 191), (41, 191), (80, 128), (320, 32)):
+        c.plan_rows(rows)
+        assert c.get_plan_info()["num_splits"] == splits, rows
+
+
 # ---------------------------------------------------------------- refusals and bookkeeping
 
 @pytest.mark.parametrize("dtype", [spk.SPK_E4M3, spk.SPK_BF16, spk.SPK_F32])

@@ -153,3 +153,32 @@ def test_eviction_over_more_pages_than_one_launch_lists():
         h.evict(0, keep, 3)
         check_pool(h, 0, keep)
     h.close()
+
+
+# ---------------------------------------------------------------- workspace
+
+@pytest.mark.parametrize("kind,heads,splits", [("e4m3", 1, 256), ("e4m3", 1, 0), ("e4m3", 16, 256), ("bf16", 2, 32), ("f32", 2, 32)])
+def test_calls_stay_inside_the_workspace(kind, heads, splits):
+    """Attention of every planned size with as many splits as it takes, weights and an eviction, in a
+    workspace of exactly the stated size: what lies behind it is not written."""
+    from budget_harness import check_attention, to_device
+    w = work(num_heads=heads, frames=300, specials_per_frame=64, patches_per_frame=16, page_size=64)
+    h = harness(w, kind, splits=splits, max_query_frames=3)
+    guard = torch.full((h.ws.numel() + (1 << 20),), 0xA5, dtype=torch.uint8, device="cuda")
+    h.ws = guard[:h.ws.numel()]
+    h.ws.zero_()
+    h.track()
+    for f in range(w.frames):
+        h.append(f)
+    for rows in (1, 32, 33, 80, 81, 240):
+        q = h.queries(rows, rows)
+        h.cache.plan_rows(rows, h.ws, h.st)
+        got = h.attend(0, q)
+        if rows in (1, 80, 240):
+            check_attention(got, h.oracle(0, q, rows), kind, f"{rows} rows")
+        lse = torch.from_numpy(got[1].astype(np.float32)).cuda()
+        h.cache.accumulate_weights(0, to_device(q, h.w.dtype), lse, h.ws, h.st)
+    h.evict(0, 10000, 2)
+    assert h.status() == 0
+    assert bool((guard[h.ws.numel():] == 0xA5).all())
+    h.close()
