@@ -52,6 +52,8 @@
 
 #include <cuda_bf16.h>
 
+#include <atomic>
+
 namespace spk {
 namespace {
 
@@ -279,7 +281,7 @@ __device__ __forceinline__ uint32_t byte_max(uint32_t v) {
   return max(v & 255u, (v >> 8) & 255u);
 }
 
-template <int D>
+template <int D, bool kPlanRegs>
 __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     attention_e4m3_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kv_map) {
   using C = Cfg<D>;
@@ -494,7 +496,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       __syncwarp();
     } else if (warp >= kWarpMain) {
       // ---------------------------------------------------------- main-tile softmax
-      ptx::regs_keep<C::kRegs>();
+      if constexpr (kPlanRegs) ptx::regs_keep<C::kRegs>();
       const int t = (warp - kWarpMain) / (4 * C::kPar), par = C::kPar == 2 ? (warp >> 2) & 1 : 0, q4 = warp & 3;
       const int r = q4 * 32 + lane;
       const int row = row0 + t * kTileRows + r;
@@ -692,7 +694,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       }
     } else if (warp < kWarpTail) {
       // ---------------------------------------------------------- widening
-      ptx::regs_keep<C::kRegs>();
+      if constexpr (kPlanRegs) ptx::regs_keep<C::kRegs>();
       bool ok = true;
       int s = 0, raw = 0;
       uint32_t phase = 0, raw_phase = 0;
@@ -724,7 +726,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       if (!ok) signal_abort(p.status, abort_flag);
     } else {
       // ---------------------------------------------------------- tail
-      ptx::regs_keep<C::kRegs>();
+      if constexpr (kPlanRegs) ptx::regs_keep<C::kRegs>();
       if (has_tail) {
         const int q = warp & 3, gr = lane >> 2, tq = lane & 3;
         const int par = q >> 1, k0 = 32 * (q & 1);  // this warp's units and its keys of them
@@ -910,21 +912,30 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   }
 }
 
-// (regs_keep names the count that the launch gives)
+// regs_keep may only name the count that a launch gives, which is the build's: ptxas takes the most that
+// the launch bounds leave, 72 and 96, with every flag tried.  A build that comes to another count runs
+// the kernel without it (2 to 7 % slower; asking in the kernel costs the same, the roles' registers are
+// then planned together).
+template <int D>
+std::atomic<bool> g_plan_regs{false};
+
 template <int D>
 cudaError_t configure_tc() {
   cudaFuncAttributes a;
-  const cudaError_t e = cudaFuncGetAttributes(&a, attention_e4m3_tc_kernel<D>);
+  cudaError_t e = cudaFuncGetAttributes(&a, attention_e4m3_tc_kernel<D, true>);
   if (e != cudaSuccess) return e;
-  if (a.numRegs != Cfg<D>::kRegs) return cudaErrorInvalidKernelImage;
-  return cudaFuncSetAttribute(attention_e4m3_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kLaunch);
+  const bool plan = a.numRegs == Cfg<D>::kRegs;
+  g_plan_regs<D> = plan;
+  return cudaFuncSetAttribute(plan ? attention_e4m3_tc_kernel<D, true> : attention_e4m3_tc_kernel<D, false>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kLaunch);
 }
 
 template <int D>
 cudaError_t launch_tc(const AttnParams& p, const CUtensorMap* map, cudaStream_t s) {
   const int64_t grid = int64_t(p.num_splits) * p.H * p.ngroups;
   if (grid <= 0 || grid > 0x7fffffff) return cudaErrorInvalidValue;
-  return launch_dependent(attention_e4m3_tc_kernel<D>, dim3(unsigned(grid)), dim3(Cfg<D>::kThreads), Cfg<D>::kLaunch, s, p, *map);
+  return launch_dependent(g_plan_regs<D> ? attention_e4m3_tc_kernel<D, true> : attention_e4m3_tc_kernel<D, false>,
+                          dim3(unsigned(grid)), dim3(Cfg<D>::kThreads), Cfg<D>::kLaunch, s, p, *map);
 }
 
 }  // namespace

@@ -182,3 +182,44 @@ def test_calls_stay_inside_the_workspace(kind, heads, splits):
     assert h.status() == 0
     assert bool((guard[h.ws.numel():] == 0xA5).all())
     h.close()
+
+
+# ---------------------------------------------------------------- builds
+
+def test_a_build_with_other_register_counts_serves_the_8_bit_cache(tmp_path):
+    """The many-row kernel plans each role's registers for the count that its launch bounds give here.
+    A build that comes to another count (here: the plan names fewer) still creates caches and computes
+    the same attention."""
+    import os
+    import shutil
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    pkg = tmp_path / "streaming_paged_kv_two_gb300"
+    shutil.copytree(os.path.join(root, "streaming_paged_kv_two_gb300"), pkg,
+                    ignore=shutil.ignore_patterns("_build", "*.so", "__pycache__"))
+    shutil.copytree(os.path.join(root, "include"), tmp_path / "include")
+    src = pkg / "csrc" / "spk_attn_e4m3_tc.cu"
+    text = src.read_text()
+    assert text.count("kRegs = D == 64 ? 72 : 96;") == 1
+    src.write_text(text.replace("kRegs = D == 64 ? 72 : 96;", "kRegs = D == 64 ? 64 : 88;"))
+    script = """
+import streaming_paged_kv_two_gb300 as spk
+assert spk.LIB_PATH.startswith(%r), spk.LIB_PATH
+from test_gpu_budget_edges import harness, work
+from budget_harness import check_attention
+for D in (64, 128):
+    w = work(head_dim=D)
+    h = harness(w, "e4m3")
+    for f in range(w.frames):
+        h.append(f)
+    q = h.queries(206, D)
+    h.cache.plan_rows(206, h.ws, h.st)
+    check_attention(h.attend(0, q), h.oracle(0, q, 206), "e4m3")
+    assert h.status() == 0
+    h.close()
+""" % str(tmp_path)
+    env = dict(os.environ, PYTHONPATH=os.pathsep.join([str(tmp_path), os.path.join(root, "tests"), root]))
+    for cmd in ([sys.executable, str(pkg / "build.py")], [sys.executable, "-c", script]):
+        r = subprocess.run(cmd, env=env, cwd=tmp_path, capture_output=True, text=True, timeout=600)
+        assert r.returncode == 0, r.stdout + r.stderr
