@@ -14,6 +14,9 @@
 // SPK_E4M3: the codes are the operand as they lie in the pool, and q, scaled by one power of two per
 // head so that its largest value is in (224, 448], is the sum of two e4m3 values (q's 8 significant
 // bits are 4 + 4): exact but for values below 2^-10 of the largest, which lose at most 2^-18 of it.
+// Where a row's largest value is more than 2^kApart below that, so that its row would lose more than
+// 2^(kApart - 18) of its own largest value to the others, each row has a power of two of its own, undone in
+// its scores (exactly; that multiplies every score: 67 us become 76, so rows near one another share one).
 // Both products go into the same accumulator; nothing is widened.  SPK_BF16: both as they are.
 //
 // Measured: 60,000 keys of 16 heads of 64 dims, 262 rows, e4m3: 62 us with the heads' sum, where the
@@ -36,6 +39,7 @@ constexpr int kThreads = 32 * (kWarpExp + 4 * kGroups);
 constexpr int kTileKeys = 128;
 constexpr int kBufCols = 128;                       // TMEM columns of a warpgroup's score buffer
 constexpr int kCols = 32;                           // scores a thread loads at a time
+constexpr int kApart = 4;                           // e4m3: see above
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int D, bool kE4m3>
@@ -53,7 +57,8 @@ struct WCfg {
   static constexpr int kQBytes = kRows * 2 * D;
   static constexpr int kK = kQBytes;
   static constexpr int kLse = kK + kStages * kTile;
-  static constexpr int kBars = kLse + kRows * 4;
+  static constexpr int kRowF = kLse + kRows * 4;     // e4m3: the rows' own factors, where they are apart
+  static constexpr int kBars = kRowF + (kE4m3 ? kRows * 4 : 0);
   // k_full, k_empty [kStages], s_full, s_free [kGroups], done [kIssuers]
   static constexpr int kMisc = kBars + 8 * (2 * kStages + 2 * kGroups + kIssuers);
   static constexpr int kBytes = kMisc + 16;
@@ -88,6 +93,12 @@ __device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
+__device__ __forceinline__ float4 lds_f4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+  return v;
+}
+
 // Four values x[0..3] scaled by s as e4m3 codes hi and the codes lo of what they leave.
 __device__ __forceinline__ void split4(const uint32_t (&bf16x2)[2], float s, uint32_t& hi, uint32_t& lo) {
   float x[4] = {__uint_as_float(bf16x2[0] << 16) * s, __uint_as_float(bf16x2[0] & 0xFFFF0000u) * s,
@@ -99,6 +110,62 @@ __device__ __forceinline__ void split4(const uint32_t (&bf16x2)[2], float s, uin
   const float2 fb = __half22float2(*reinterpret_cast<const __half2*>(&b));
   lo = uint32_t(__nv_cvt_float2_to_fp8x2(make_float2(x[0] - fa.x, x[1] - fa.y), __NV_SATFINITE, __NV_E4M3)) |
        uint32_t(__nv_cvt_float2_to_fp8x2(make_float2(x[2] - fb.x, x[3] - fb.y), __NV_SATFINITE, __NV_E4M3)) << 16;
+}
+
+// Largest finite magnitude of a row, whose D / 8 consecutive lanes hold 8 values each (fp32 bits).
+template <int D>
+__device__ __forceinline__ uint32_t row_amax(uint4 v) {
+  const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+  uint32_t amax = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t a = (x[j] << 16) & 0x7FFFFFFFu, b = x[j] & 0x7FFF0000u;
+    amax = max(amax, max(a < 0x7F800000u ? a : 0u, b < 0x7F800000u ? b : 0u));
+  }
+#pragma unroll
+  for (int o = 1; o < D / 8; o *= 2) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  return amax;
+}
+
+// k with 2^k |q| in (224, 448]: with |q| = 1.m 2^(E - 127), k = 8 - (E - 127) - (1.m > 1.75)
+__device__ __forceinline__ int scale_exponent(uint32_t amax) {
+  return amax == 0 ? 0 : min(max(135 - int(amax >> 23) - ((amax & 0x7FFFFFu) > 0x600000u ? 1 : 0), -120), 120);
+}
+
+// Sum over `cols` score columns of 2^(a s f + m): m and f one value a column at shared addresses m_at and
+// f_at (f = 1 without kOwnFactors).  Arrives at `free_bar` once the scores are in registers.
+template <bool kOwnFactors>
+__device__ __forceinline__ float add_terms(uint32_t tS, uint32_t m_at, uint32_t f_at, float a, int cols, uint32_t free_bar) {
+  float h0 = 0.f, h1 = 0.f;
+#pragma unroll 1
+  for (int j = 0; j < cols; j += kCols) {
+    uint32_t s[kCols];
+    ptx::tmem_ld32(tS + uint32_t(j), s);
+    ptx::tmem_wait_ld();
+    if (j + kCols >= cols) {
+      ptx::tc_fence_before();
+      e4m3::arrive_warp(free_bar);
+    }
+#pragma unroll
+    for (int e = 0; e < kCols; e += 4) {
+      float x0 = __uint_as_float(s[e]), x1 = __uint_as_float(s[e + 1]), x2 = __uint_as_float(s[e + 2]),
+            x3 = __uint_as_float(s[e + 3]);
+      const float4 m = lds_f4(m_at + uint32_t(4 * (j + e)));
+      if constexpr (kOwnFactors) {
+        const float4 f = lds_f4(f_at + uint32_t(4 * (j + e)));
+        x0 *= f.x, x1 *= f.y, x2 *= f.z, x3 *= f.w;
+      }
+      ptx::fma2(x0, x1, x0, x1, a, m.x, m.y);
+      ptx::fma2(x2, x3, x2, x3, a, m.z, m.w);
+      ptx::add2(h0, h1, ptx::ex2(x0), ptx::ex2(x1));
+      ptx::add2(h0, h1, ptx::ex2(x2), ptx::ex2(x3));
+    }
+  }
+  return h0 + h1;
+}
+// (out of line: inlined beside the common path it costs that 3 of 67 us, so 1)
+__device__ __noinline__ float add_terms_apart(uint32_t tS, uint32_t m_at, uint32_t f_at, float a, int cols, uint32_t free_bar) {
+  return add_terms<true>(tS, m_at, f_at, a, cols, free_bar);
 }
 
 template <int D, bool kE4m3>
@@ -115,9 +182,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto s_free = [&](int i) { return sbase + uint32_t(C::kBars + 8 * (2 * S + kGroups + i)); };
   auto done = [&](int i) { return sbase + uint32_t(C::kBars + 8 * (2 * S + 2 * kGroups + i)); };
   float* neg_lse = reinterpret_cast<float*>(smem + C::kLse);
+  float* row_f = reinterpret_cast<float*>(smem + C::kRowF);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMisc + 4);
-  uint32_t* q_amax = reinterpret_cast<uint32_t*>(smem + C::kMisc + 8);
+  uint32_t* q_amax = reinterpret_cast<uint32_t*>(smem + C::kMisc + 8);   // of all rows
+  uint32_t* q_least = reinterpret_cast<uint32_t*>(smem + C::kMisc + 12);  // of the row with the smallest but 0
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const WeightParams& w = p.w;
@@ -135,6 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kIssuers; ++i) ptx::mbar_init(done(i), 1);
     *abort_flag = 0;
     *q_amax = 0;
+    *q_least = 0xFFFFFFFFu;
     ptx::fence_mbar_init();
     ptx::fence_proxy_async_smem();
   }
@@ -154,7 +224,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tiles = (units + kPerTile - 1) / kPerTile;
   const int t0 = int(int64_t(tiles) * blockIdx.x / p.splits), t1 = int(int64_t(tiles) * (blockIdx.x + 1) / p.splits);
   const int n = t1 - t0;
-  // the rows' largest |q|, one power of two for all of them
   const int64_t q_stride = int64_t(w.H) * D;
   const __nv_bfloat16* q0 =
       static_cast<const __nv_bfloat16*>(w.q) + (int64_t(stream) * w.T + p.row0) * q_stride + int64_t(head) * D;
@@ -163,36 +232,45 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kPieces = D / 8;  // 16-byte pieces of a bf16 row
   const int padded = p.groups * p.group_rows;
   if (n > 0) {
-    float scale = 1.f;
+    // (past the last row: that row again, at weight 0 below.  Zeros would turn an infinite key's score
+    // into a NaN that no row has.)
+    auto piece_of = [&](int i) {
+      return __ldg(reinterpret_cast<const uint4*>(q0 + min(i / kPieces, p.rows - 1) * q_stride) + i % kPieces);
+    };
+    // (padded rows are whole warps of pieces, which take each step together)
     if constexpr (kE4m3) {
-      uint32_t amax = 0;
-      for (int i = threadIdx.x; i < p.rows * kPieces; i += kThreads) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(q0 + (i / kPieces) * q_stride) + i % kPieces);
-        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t a = (x[j] << 16) & 0x7FFFFFFFu, b = x[j] & 0x7FFF0000u;
-          amax = max(amax, max(a < 0x7F800000u ? a : 0u, b < 0x7F800000u ? b : 0u));  // finite values
-        }
+      uint32_t amax = 0, least = 0xFFFFFFFFu;
+      for (int i = threadIdx.x; i < padded * kPieces; i += kThreads) {
+        const uint32_t a = row_amax<D>(piece_of(i));
+        amax = max(amax, a);
+        if (a) least = min(least, a);
       }
       amax = __reduce_max_sync(0xffffffffu, amax);
-      if (lane == 0) atomicMax(q_amax, amax);
+      least = __reduce_min_sync(0xffffffffu, least);
+      if (lane == 0) {
+        atomicMax(q_amax, amax);
+        atomicMin(q_least, least);
+      }
     }
     __syncthreads();
     float factor = w.scale_log2;  // score of a key: factor (its scale) (product)
+    int k_head = 0;
+    bool apart = false;
     if constexpr (kE4m3) {
-      // 2^k |q| in (224, 448]: with |q| = 1.m 2^(E - 127), k = 8 - (E - 127) - (1.m > 1.75)
-      const uint32_t a = *q_amax;
-      const int k = a == 0 ? 0 : min(max(135 - int(a >> 23) - ((a & 0x7FFFFFu) > 0x600000u ? 1 : 0), -120), 120);
-      scale = __uint_as_float(uint32_t(127 + k) << 23);
-      factor *= __uint_as_float(uint32_t(127 - k) << 23);
+      k_head = scale_exponent(*q_amax);
+      factor *= __uint_as_float(uint32_t(127 - k_head) << 23);
+      apart = *q_amax > 0 && scale_exponent(*q_least) - k_head > kApart;
     }
-    for (int i = threadIdx.x; i < padded * (D / 8); i += kThreads) {
-      const int r = i / (D / 8), c = i % (D / 8);
-      // (past the last row: that row again, at weight 0 below.  Zeros would turn an infinite key's
-      // score into a NaN that no row has.)
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(q0 + min(r, p.rows - 1) * q_stride) + c);
+    for (int i = threadIdx.x; i < padded * kPieces; i += kThreads) {
+      const int r = i / kPieces, c = i % kPieces;
+      const uint4 v = piece_of(i);
       if constexpr (kE4m3) {
+        int k = k_head;
+        if (apart) {
+          k = min(max(scale_exponent(row_amax<D>(v)), k_head), k_head + 126);
+          if (c == 0) row_f[r] = __uint_as_float(uint32_t(127 + k_head - k) << 23);
+        }
+        const float scale = __uint_as_float(uint32_t(127 + k) << 23);
         const uint32_t x0[2] = {v.x, v.y}, x1[2] = {v.z, v.w};
         uint32_t hi[2], lo[2];
         split4(x0, scale, hi[0], lo[0]);
@@ -323,29 +401,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t tS = tmem + uint32_t(wg * kBufCols) + (uint32_t(q4 * 32) << 16);
           // (columns past the last row of the pass weigh nothing)
           const int cols = min(p.group_rows, p.rows - g * p.group_rows);
-          float h0 = 0.f, h1 = 0.f;
-#pragma unroll 1
-          for (int j = 0; j < cols; j += kCols) {
-            uint32_t s[kCols];
-            ptx::tmem_ld32(tS + uint32_t(j), s);
-            ptx::tmem_wait_ld();
-            if (j + kCols >= cols) {  // the scores are in registers
-              ptx::tc_fence_before();
-              e4m3::arrive_warp(s_free(wg));
-            }
-#pragma unroll
-            for (int e = 0; e < kCols / 4; ++e) {
-              float m0, m1, m2, m3, x0, x1, x2, x3;
-              asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                           : "=f"(m0), "=f"(m1), "=f"(m2), "=f"(m3)
-                           : "r"(nl + uint32_t(4 * (g * p.group_rows + j + 4 * e))));
-              ptx::fma2(x0, x1, __uint_as_float(s[4 * e]), __uint_as_float(s[4 * e + 1]), a, m0, m1);
-              ptx::fma2(x2, x3, __uint_as_float(s[4 * e + 2]), __uint_as_float(s[4 * e + 3]), a, m2, m3);
-              ptx::add2(h0, h1, ptx::ex2(x0), ptx::ex2(x1));
-              ptx::add2(h0, h1, ptx::ex2(x2), ptx::ex2(x3));
-            }
-          }
-          sum += h0 + h1;
+          const uint32_t m = nl + uint32_t(4 * g * p.group_rows);
+          if (kE4m3 && apart) sum += add_terms_apart(tS, m, m + uint32_t(C::kRowF - C::kLse), a, cols, s_free(wg));
+          else sum += add_terms<false>(tS, m, 0, a, cols, s_free(wg));
         }
         if (ok && valid) {
           float* dst = w.part + (int64_t(stream) * w.H + head) * w.cap + pos;

@@ -111,6 +111,58 @@ def test_keys_of_minus_infinite_score_weigh_nothing(kind, D, rows):
     h.close()
 
 
+def weight_bounds(q, k, lse, e4m3):
+    """(exact sum, bound of its error) per key: q [R, H, D], k [n, H, D], lse [R, H] in 64 bits.
+
+    A term exp(s - lse) is off by the fp32 rounding of its exponent: the score's (D + 8 roundings of the
+    absolute sum of its products, twice: product and scaling), the log-sum-exp's (twice), 2^-20 for the
+    exponential and its argument.  An 8-bit cache's q is two e4m3 values under a power of two that puts
+    the row's largest value at 224 or more, or up to 16 times lower where the rows of the head share one: an
+    element of more than 2^-10 of the head's largest is exact, another is off by half a step of 2^-9 of
+    what the head's largest is at least 224 of.  The sum adds a rounding for each of its levels."""
+    R, H, D = q.shape
+    rows, big = np.abs(q).max(-1), np.abs(q).max((0, 2))                      # [R, H], [H]
+    apart = (rows > 0) & (rows < big * 2.0 ** -5)
+    ref = np.where(apart.any(0), rows, big)                                   # [R, H]: whose 224 counts
+    loss = np.where(np.abs(q) < ref[..., None] * 2.0 ** -9, ref[..., None] * 2.0 ** -10 / 224, 0.0) if e4m3 else 0 * q
+    total, bound = np.zeros(len(k)), np.zeros(len(k))
+    for h in range(H):
+        p = np.exp(q[:, h] @ k[:, h].T / np.sqrt(D) - lse[:, h, None])        # [R, n]
+        ds = ((np.abs(q[:, h]) * (2 * (D + 8) * 2.0 ** -24) + loss[:, h]) @ np.abs(k[:, h]).T) / np.sqrt(D)
+        total += p.sum(0)
+        bound += (p * (ds + np.abs(lse[:, h, None]) * 2.0 ** -22 + 2.0 ** -20)).sum(0)
+    return total, bound + total * (R / 16 + 40 + H) * 2.0 ** -24
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("big", [2.0 ** 5, 2.0 ** 9, 2.0 ** 13])
+def test_a_row_far_above_the_others_takes_nothing_from_them(D, big):
+    """One query row of a head far larger than the rest (and a row of zeros): the others' terms are as
+    exact as they are without it."""
+    from budget_harness import to_device
+    w = work(head_dim=D, num_heads=2, frames=40)
+    h = harness(w, "e4m3")
+    h.track()
+    for f in range(w.frames):
+        h.append(f)
+    rows = 70
+    q = wl.to_f64(h.queries(rows, 3), "bf16").astype(np.float32)
+    q[33, 1] *= np.float32(big)
+    q[50] = 0
+    q = wl.f32_to_bf16_bits(q)
+    x = wl.to_f64(q, "bf16")
+    lse = np.full((rows, 2), 5.0)
+    lse[33, 1] = 1e5 if big > 2.0 ** 9 else 5e4 if big > 32 else 500.0       # (its own terms are 0)
+    h.cache.plan_rows(rows, h.ws, h.st)
+    h.cache.accumulate_weights(0, to_device(q, "bf16"), torch.from_numpy(lse.astype(np.float32)).cuda(), h.ws, h.st)
+    k = np.stack([r[0] for r in h.special[(0, 0)]])
+    exact, bound = weight_bounds(x, k, lse, True)
+    worst = (np.abs(h.weights[0, :len(k)].double().cpu().numpy() - exact) / bound).max()
+    assert worst <= 1, worst
+    assert h.status() == 0
+    h.close()
+
+
 # ---------------------------------------------------------------- eviction
 
 def test_evictions_of_many_streams_do_not_wait_for_the_gpu():
