@@ -134,6 +134,69 @@ def weight_bounds(q, k, lse, e4m3):
     return total, bound + total * (R / 16 + 40 + H) * 2.0 ** -24
 
 
+@pytest.mark.parametrize("kind", ["e4m3", "bf16"])
+@pytest.mark.parametrize("rows,D", [(8, 64), (8, 128), (150, 64), (150, 128)])
+def test_weights_of_long_records(kind, rows, D):
+    """Records long enough that each of the two CTAs of a (stream, head) walks its ring of 128-key tiles
+    several times with every warpgroup (some 25 tiles), pages that end inside a tile, and a stream that holds far fewer tokens than the others."""
+    from budget_harness import to_device
+    w = work(num_streams=4, num_heads=16, head_dim=D, frames=80, specials_per_frame=61, patches_per_frame=90,
+             page_size=200, sliding_window=1)
+    h = harness(w, kind)
+    h.track()
+    for f in range(w.frames):
+        h.append(f)
+    h.weights[1, :w.frames * 61] = torch.rand(w.frames * 61, device="cuda", generator=torch.Generator("cuda").manual_seed(1))
+    h.evict(1, 700, 2)
+    g = np.random.default_rng(rows)
+    q = h.queries(rows, rows, 1.5)
+    lse = g.uniform(2, 6, (4 * rows, 16)).astype(np.float32)
+    before = h.weights.clone()
+    h.cache.plan_rows(rows, h.ws, h.st)
+    h.cache.accumulate_weights(0, to_device(q, "bf16"), torch.from_numpy(lse).cuda(), h.ws, h.st)
+    assert h.status() == 0
+    for s in range(4):
+        n = len(h.special[(s, 0)])
+        assert n == (700 if s == 1 else 4880)
+        assert torch.equal(h.weights[s, n:], before[s, n:])       # behind the last token: untouched
+        at = np.unique(np.concatenate([np.arange(n - 140, n), g.integers(0, n, 400)]))
+        k = np.stack([h.special[(s, 0)][i][0] for i in at])
+        r = slice(s * rows, (s + 1) * rows)
+        exact, bound = weight_bounds(wl.to_f64(q[r], "bf16"), k, lse[r].astype(np.float64), kind == "e4m3")
+        was = before[s].double().cpu().numpy()[at]
+        got = h.weights[s].double().cpu().numpy()[at]
+        worst = (np.abs(got - was - exact) / (bound + (was + exact) * 2.0 ** -24)).max()
+        assert worst <= 1, (s, worst)
+    h.close()
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "bf16", "f32"])
+@pytest.mark.parametrize("rows,D", [(769, 64), (800, 64), (1600, 64), (385, 128), (800, 128)])
+def test_weights_of_more_rows_than_one_pass_holds(kind, rows, D):
+    from budget_harness import to_device
+    w = work(num_streams=2, num_heads=3, head_dim=D, frames=9, specials_per_frame=64, patches_per_frame=16, page_size=100)
+    h = harness(w, kind, max_query_frames=20)
+    h.track()
+    for f in range(w.frames):
+        h.append(f)
+    q = h.queries(rows, rows, 1.5)
+    x = wl.to_f64(q, h.w.dtype).astype(np.float32)
+    x[:rows // 2] *= np.float32(4)                       # the passes' largest values differ
+    q = wl.f32_to_bf16_bits(x) if kind != "f32" else x
+    lse = np.random.default_rng(rows).uniform(20, 24, (2 * rows, 3)).astype(np.float32)
+    h.cache.plan_rows(rows, h.ws, h.st)
+    h.cache.accumulate_weights(0, to_device(q, h.w.dtype), torch.from_numpy(lse).cuda(), h.ws, h.st)
+    assert h.status() == 0
+    for s in range(2):
+        n = len(h.special[(s, 0)])
+        r = slice(s * rows, (s + 1) * rows)
+        k = np.stack([x[0] for x in h.special[(s, 0)]])
+        exact, bound = weight_bounds(wl.to_f64(q[r], h.w.dtype), k, lse[r].astype(np.float64), kind == "e4m3")
+        worst = (np.abs(h.weights[s, :n].double().cpu().numpy() - exact) / bound).max()
+        assert worst <= 1, (s, worst)
+    h.close()
+
+
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("big", [2.0 ** 5, 2.0 ** 9, 2.0 ** 13])
 def test_a_row_far_above_the_others_takes_nothing_from_them(D, big):
