@@ -58,7 +58,7 @@ enum spk_status {
   SPK_OK = 0,
   SPK_ERR_INVALID_ARG = 1,          /* bad pointer, size, id or configuration */
   SPK_ERR_OUT_OF_PATCH_PAGES = 2,   /* no free patch page for a new frame */
-  SPK_ERR_OUT_OF_SPECIAL_PAGES = 3, /* every special page is full: the special stream only grows */
+  SPK_ERR_OUT_OF_SPECIAL_PAGES = 3, /* every special page is full: the special stream grows until spk_evict_specials */
   SPK_ERR_BAD_STATE = 4,            /* wrong call order: block order, stale or missing plan */
   SPK_ERR_CUDA = 5,                 /* a CUDA runtime/driver call failed */
   SPK_ERR_DEVICE_TIMEOUT = 6        /* a device-side wait ran past its limit; see spk_read_device_status */
@@ -83,9 +83,13 @@ enum spk_dtype {
  *     be rewritten, and their codes with it.
  *   - max|x| is taken over the finite values; an infinity is stored as +-448 s, a NaN as NaN.
  *   - The scales being powers of two, code * scale is exact in fp32 (and bf16).
- * Attention rounds each softmax weight to fp16 (2^-11) and sums in fp32.  What fp16's range cannot
- * hold beside the largest value is lost: a part of the output below 2^-32 of the head's largest
- * visible |v|, a weight below 2^-32 of the row's largest. */
+ * Attention rounds each softmax weight to fp16 and sums in fp32.  fp16 keeps 2^-11 of a weight while
+ * that is a normal number, and below that a fixed step: a weight is off by 2^-11 of itself or by 2^-32
+ * of the row's largest weight, whichever is more (so below 2^-32 it is lost), and the output, before its
+ * rounding to bf16, by the sum of that over the N visible keys: at most 2^-11 of sum(p |v|) plus
+ * (N + 1) 2^-32 of the head's largest visible |v|.  With more than 32 query rows K is fp16 too, beside
+ * the largest scale of a KV split: exact but for elements more than 2^15 below that, and a score moves by
+ * at most 2^-32 of sum(|q|) max|k| / sqrt(D), k any visible key of the head. */
 
 typedef struct {
   int32_t num_blocks;          /* L: one pool per transformer block */
@@ -116,7 +120,7 @@ typedef struct {
   int64_t scale_pages;     /* patch pages held as scale frames */
   int64_t live_pages;      /* patch pages in the live window */
   int64_t free_pages;      /* free patch pages */
-  int64_t special_tokens;  /* special tokens appended (S per frame) */
+  int64_t special_tokens;  /* special tokens held: S per frame, less those evicted (spk_evict_specials) */
 } spk_stats;
 
 typedef struct {
@@ -308,7 +312,8 @@ int spk_run_attention_lse(spk_cache* cache, int block, const void* q, void* out,
  * cache is destroyed.  Entry i belongs to the stream's special token at position i (position i
  * lives in slot i % page_size of the stream's (i / page_size)-th special page).  ids holds the
  * token's arrival number (frame * S + row modulo 2^32, frames counted from 0 at create or reset); weights
- * what spk_accumulate_weights has added.  Tokens already held get weight 0 and their numbers
+ * what spk_accumulate_weights has added (a rolled-back frame takes its own tokens' records with it, not
+ * what its rows have added to others).  Tokens already held get weight 0 and their numbers
  * here; every later block-0 append does so for its frame (one small kernel).
  * SPK_ERR_BAD_STATE when special tokens have already been evicted (their numbers are only in
  * the records).  On a bookkeeping-only cache both are NULL.  Work is ordered on cuda_stream. */
@@ -317,7 +322,9 @@ int spk_track_specials(spk_cache* cache, float* weights, int32_t* ids, void* cud
 /* Add to each special token's weight the attention it receives from the query rows of one
  * block: weights[s][j] += sum over heads h and rows i of exp(q_ih k_jh / sqrt(D) - lse_ih).
  * q: as given to spk_run_attention for this block; lse: device fp32 [B*T, H], the rows'
- * log-sum-exps over all visible keys (spk_run_attention_lse of the same plan).  The sums do
+ * log-sum-exps over all visible keys (spk_run_attention_lse of the same plan).  Scores are fp32 sums of
+ * q and K as they are stored; SPK_E4M3 takes q in two e4m3 terms, exact but for elements below 2^-5 of
+ * the row's largest, which lose at most 2^-13 of it.  The sums do
  * not depend on the order of execution: two equal calls add the same bits.  Requires tracking
  * (spk_track_specials), a current plan and the block appended, like spk_run_attention.  Calls that
  * are given one workspace use the same scratch: their GPU work runs in order (one stream, or
@@ -329,7 +336,8 @@ int spk_accumulate_weights(spk_cache* cache, int block, const void* q, const flo
 
 /* Evict special tokens of one stream down to `keep` by accumulated weight; nothing happens
  * while it holds at most `keep`.  Tokens of the last recent_frames frames (by arrival number,
- * the current frame included) are kept; of the others the (held - keep) of least weight leave,
+ * the current frame included) are kept (and so is one that has outlived 2^31 younger arrivals: the
+ * numbers wrap); of the others the (held - keep) of least weight leave,
  * the lowest position first among equals (a NaN weighs more than any number).  Survivors at
  * positions >= keep move, in ascending order, into the vacated positions < keep, in ascending
  * order, with their K/V (and scales) in every block's pool, weight and id; no other slot is

@@ -14,8 +14,9 @@
 //   its scores in fp32.
 //   O += P' V: P' = p 2^(b_v - R) 2^12 in fp16, p <= 1 the softmax weight against the running
 //   maximum and R the running largest scale byte.  The scale of V thus enters once, exactly,
-//   and 2^12 puts P' high in fp16's range: what lies more than 2^36 below the largest term is
-//   lost, the rest is rounded by 2^-11 relative at most.  Row sums are those of the fp32 p.
+//   and 2^12 puts P' high in fp16's range: it is rounded by 2^-11 of itself down to 2^-14 (2^-26 of
+//   the largest there can be), below that by up to 2^-25, which times a code of at most 448 is 2^-36
+//   of the largest |v| a key.  Row sums are those of the fp32 p.
 // The order of a warp product's contraction is free, so each thread takes 16 consecutive dims
 // of a key (one 16-byte shared-memory load) for Q K^T, and 8 or 16 consecutive dims of its four
 // keys for P V; the swizzle of the copies keeps both free of bank conflicts (D = 128's K: two-way).

@@ -6,12 +6,13 @@
 //
 // Operands.  The codes are widened to fp16 in shared memory once per CTA and unit, with their
 // scales: K' = c 2^(b - RK), V' = c 2^(b - RV), RK and RV the largest scale bytes of the split, so
-// that |K'|, |V'| <= 448 (exact but for values below 2^-24; fp16 because 8-bit weights would cost
-// the output four bits and bf16 three).  Q' = q 2^(127 - e) with the row's largest value in [1, 2).
-// Scores are x = rf (Q' K') in log2 units, rf = log2(e) / sqrt(D) 2^(e - 127) 2^(RK - 127) one
-// factor per row; P' = 2^(x - m + 8) in fp16 with m a running maximum that moves only when 32 P' sum
-// to 2^14 (a score 6 above m at the latest): a weight below 2^-32 of the row's largest is lost, the others
-// are rounded by 2^-11.  Row sums are taken from the fp32 weights.
+// that |K'|, |V'| <= 448 (exact down to 2^-15 of the largest scale, below that rounded by up to 2^-25;
+// fp16 because 8-bit weights would cost the output four bits and bf16 three).  Q' = q 2^(127 - e) with
+// the row's largest value in [1, 2).  Scores are x = rf (Q' K') in log2 units, rf = log2(e) / sqrt(D)
+// 2^(e - 127) 2^(RK - 127) one factor per row; P' = 2^(x - m + 8) in fp16 with m a running maximum that
+// moves only when 32 P' sum to 2^14 (a score 6 above m at the latest).  The row's largest P' is thus at
+// least 2^7; a P' is rounded by 2^-11 of itself down to 2^-14, below that by up to 2^-25: 2^-32 of the
+// row's largest weight.  Row sums are taken from the fp32 weights.
 //
 // Warps:
 //   0-3    widen the units;
