@@ -108,8 +108,9 @@ typedef struct {
                                   for SPK_E4M3, to 256 while the plan's rows allow it: see max_query_frames) */
   int32_t max_query_frames;    /* most frames of queries one attention call may carry (spk_plan_queries);
                                   0 or 1 = one frame per call.  Sizes the workspace's split partials: 32 splits of that many
-                                  frames' rows, SPK_E4M3 also up to 256 (fewer with many heads and streams) of one
-                                  frame's.  Plans of SPK_E4M3 caches take as many splits as fit. */
+                                  frames' rows; SPK_E4M3 at least up to 256 (fewer with many heads and streams) of one
+                                  frame's, and 77,824 rows over all streams, heads and splits.  Plans of SPK_E4M3
+                                  caches take as many splits as fit. */
   const int32_t* patch_page_order;   /* optional host array [B*MPP]: initial free-list order, global ids;
                                         entries [s*MPP, (s+1)*MPP) must permute stream s's patch ids. NULL = ascending */
   const int32_t* special_page_order; /* optional host array [B*MSP], same rule for special ids. NULL = ascending */

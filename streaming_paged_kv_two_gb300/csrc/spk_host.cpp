@@ -147,11 +147,14 @@ WorkspaceLayout make_layout(const spk_config& c) {
   L.works = off;   off = align256(off + sizeof(WorkDesc) * L.max_splits);
   L.plan_end = off;
   const int64_t Tq = T * std::max(1, c.max_query_frames);  // query rows per stream of the largest plan
-  // Split partials.  More splits than kMaxSplitsPerStream serve calls of few rows (one frame's, or
-  // those of the rows kernel), so rows times splits is what is bounded (split_limit).
+  // Split partials.  More splits than kMaxSplitsPerStream serve calls that have few CTAs without them:
+  // few rows (one frame's, or those of the rows kernel) or few streams and heads (enough for kE4m3Ctas
+  // CTAs of 128 rows), so rows times splits is what is bounded (split_limit).
   L.part_rows = kMaxSplitsPerStream * Tq;
   if (c.dtype == SPK_E4M3)
-    L.part_rows = std::max(L.part_rows, L.max_splits_per_stream * std::min(Tq, std::max<int64_t>(T, kE4m3RowsMost)));
+    L.part_rows = std::max(L.part_rows, std::min(L.max_splits_per_stream * Tq,
+                                                 std::max(L.max_splits_per_stream * std::max<int64_t>(T, kE4m3RowsMost),
+                                                          int64_t(kE4m3Ctas) * kTileRows / (B * c.num_heads))));
   const size_t rows = size_t(B) * size_t(L.part_rows) * c.num_heads;
   L.part_o = off;
   L.part_lse = align256(L.part_o + sizeof(float) * rows * c.head_dim);

@@ -102,17 +102,21 @@ def test_workspace_holds_no_scratch_of_its_own_for_the_budget(dtype):
 
 
 def test_splits_follow_the_planned_rows():
-    """200 forced splits: every chunk of 3 patch and 188 special pages for a row and for a frame, as many
-    as the partials hold (10,240 rows) for two and for eight."""
-    cfg, _ = make(num_heads=1, patches_per_frame=30, specials_per_frame=10, page_size=64, max_special_pages=200,
+    """200 forced splits: as many as eight heads may have (608 / 8) for up to two frames' rows, as many as
+    the partials hold (10,240 rows a stream and head: 32 splits of eight frames) for more.  One head
+    may have them all (3 patch and 188 special pages): its partials hold 77,824 rows."""
+    cfg, _ = make(num_heads=8, patches_per_frame=30, specials_per_frame=10, page_size=64, max_special_pages=200,
                   splits_per_stream=200, max_query_frames=8)
-    c = spk.Cache(cfg)
-    for _ in range(1200):
-        c.append_frame(0, 0)
-        c.evict_frames(0)
-    for rows, splits in ((1, 191), (40, 191), (41, 191), (80, 128), (320, 32)):
-        c.plan_rows(rows)
-        assert c.get_plan_info()["num_splits"] == splits, rows
+    one, _ = make(num_heads=1, patches_per_frame=30, specials_per_frame=10, page_size=64, max_special_pages=200,
+                  splits_per_stream=200, max_query_frames=8)
+    for cfg, wanted in ((cfg, ((1, 76), (40, 76), (80, 76), (160, 64), (320, 32))), (one, ((1, 191), (320, 191)))):
+        c = spk.Cache(cfg)
+        for _ in range(1200):
+            c.append_frame(0, 0)
+            c.evict_frames(0)
+        for rows, splits in wanted:
+            c.plan_rows(rows)
+            assert c.get_plan_info()["num_splits"] == splits, rows
 
 
 # ---------------------------------------------------------------- refusals and bookkeeping
