@@ -47,7 +47,7 @@ struct RowsCfg {
   static constexpr int kTile = kUnitTokens * D;      // codes of one K or V stage
   static constexpr int kScales = 2 * kUnitTokens;    // K then V scale bytes
   // about 200 KB in flight per SM: two CTAs, but one for 16 rows of 128 dims (whose registers
-  // would not fit twice)
+  // would not fit twice; ptxas spills 12 to 20 bytes a thread, none for 8 rows of 64 dims)
   static constexpr int kCtas = D == 128 && kRows == 16 ? 1 : 2;
   static constexpr int kStages = D == 128 && kCtas == 2 ? 6 : 12;
   static constexpr int kPairs = kStages == 6 ? 3 : 4;  // of consumer warps, which take the stages in turn

@@ -78,7 +78,8 @@ struct Cfg {
   static constexpr int kWarpTma = kWarpMain + 8 * kPar;
   static constexpr int kWarpMma = kWarpTma + 1;
   static constexpr int kThreads = 32 * (kWarpMma + 2);
-  static constexpr int kRegs = D == 64 ? 72 : 96;     // registers a thread (7 or 5 warps on an SM sub-partition)
+  // registers a thread (7 or 5 warps on an SM sub-partition; D = 64 spills 4 bytes)
+  static constexpr int kRegs = D == 64 ? 72 : 96;
   static constexpr int kTile = kUnit * D * 2;         // one widened K' or V' unit
   static constexpr int kBlock = kUnit * 128;          // its 64-column block (128-byte rows)
   static constexpr int kRawTile = kUnit * D;
