@@ -40,8 +40,9 @@
 // A unit's slot is free once every consumer's P V of it has completed (slot_free, which the rare
 // path that moves m waits on too).  Every wait is bounded, as in the bf16 kernel.
 //
-// Measured with the merge: 78,432 keys of 16 heads of 64 dims, 262 rows 112 us (753 TFLOP/s); 51,960
-// keys, 1005 rows 270 us (793); 4 x 63,792 keys of 8 heads of 128 dims, 262 rows 271 us (1,010).
+// Measured with the merge: 78,432 keys of 16 heads of 64 dims, 262 rows 113 to 118 us (747 to 715
+// TFLOP/s; 107 where scores spread so little that m hardly moves); 51,960 keys, 1005 rows 271 to 278 us
+// (790 to 770; 261); 4 x 63,792 keys of 8 heads of 128 dims, 262 rows 272 to 276 us (1,005 to 990; 270).
 // DRAM is at 6 to 27 %, the tensor pipe at 38 to 53 %.  A unit of 64 dims takes some 1,350 cycles:
 // 520 of products, 720 of exponentials and packing at the rate of four warps by themselves, 66 % of the
 // issue slots; the softmax warps and the widening warps are both busy all the time, a third of it with

@@ -19,9 +19,10 @@
 // scores (exactly; that multiplies every score: 67 us become 76, so rows near one another share one).
 // Both products go into the same accumulator; nothing is widened.  SPK_BF16: both as they are.
 //
-// Measured: 60,000 keys of 16 heads of 64 dims, 262 rows, e4m3: 62 us with the heads' sum, where the
-// exponentials alone would take 31 (16 scores a load: 66 us; 16 scores loaded ahead of their use:
-// 68; more score buffers or more issuers, measured with slower issuers: 77 to 80); 1,200 keys, bf16: 9 us.
+// Measured: 60,000 keys of 16 heads of 64 dims, 262 rows, e4m3: 61 us with the heads' sum over one set of
+// inputs, 68 over inputs that change, where the exponentials alone would take 31 (16 scores a load: 4 us
+// more; 16 scores loaded ahead of their use: 6; more score buffers or more issuers, measured with slower
+// issuers: 15 to 18); bf16 60; 1,200 keys, bf16: 9 us.
 #include "ptx_sm100.cuh"
 #include "spk_e4m3.cuh"
 #include "spk_internal.h"
