@@ -299,6 +299,48 @@ def test_calls_stay_inside_the_workspace(kind, heads, splits):
     h.close()
 
 
+@pytest.mark.parametrize("kind", ["e4m3", "bf16"])
+def test_pages_past_four_gigabytes(kind, monkeypatch):
+    """The stream's special pages at the end of a pool of 5.5 (bf16: 11) GB: attention, weights and an
+    eviction address them and their scales."""
+    import budget_harness
+    from budget_harness import check_attention, to_device
+    from test_gpu_budget import check_pool
+    import streaming_paged_kv_two_gb300 as spk
+
+    def config(w, splits, max_query_frames):
+        pages = 1300
+        return spk.make_config(
+            num_blocks=1, num_streams=1, num_heads=16, head_dim=128, page_size=1024,
+            patches_per_frame=w.patches_per_frame, specials_per_frame=w.specials_per_frame,
+            scale_frames=w.scale_frames, sliding_window=w.sliding_window, max_patch_pages=8, max_special_pages=pages,
+            dtype=spk.SPK_BF16, splits_per_stream=splits, max_query_frames=max_query_frames,
+            special_page_order=list(range(8 + pages - 1, 7, -1)))
+
+    monkeypatch.setattr(budget_harness, "spk_config_for", config)
+    w = work(num_heads=16, head_dim=128, frames=25, specials_per_frame=64, page_size=1024)
+    h = harness(w, kind)
+    assert h.pools[0].numel() > 2 ** 32
+    h.track()
+    for f in range(w.frames):
+        h.append(f)
+    for rows in (1, 40):
+        q = h.queries(rows, rows)
+        h.cache.plan_rows(rows, h.ws, h.st)
+        got = h.attend(0, q)
+        check_attention(got, h.oracle(0, q, rows), kind, f"{rows} rows")
+    n = w.frames * 64
+    lse = np.full((40, 16), 6.0, np.float32)
+    h.cache.accumulate_weights(0, to_device(q, "bf16"), torch.from_numpy(lse).cuda(), h.ws, h.st)
+    exact, bound = weight_bounds(wl.to_f64(q, "bf16"), np.stack([r[0] for r in h.special[(0, 0)]]), lse.astype(np.float64),
+                                 kind == "e4m3")
+    assert (np.abs(h.weights[0, :n].double().cpu().numpy() - exact) / bound).max() <= 1
+    h.evict(0, 1100, 2)
+    check_pool(h, 0)
+    assert h.status() == 0
+    h.close()
+
+
 # ---------------------------------------------------------------- builds
 
 def test_a_build_with_other_register_counts_serves_the_8_bit_cache(tmp_path):
