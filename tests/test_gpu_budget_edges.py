@@ -270,6 +270,50 @@ def test_eviction_over_more_pages_than_one_launch_lists():
     h.close()
 
 
+# ---------------------------------------------------------------- attention
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("rows", [3, 8, 16, 31, 136, 206])
+def test_a_nan_stays_where_it_is(D, rows):
+    """A NaN or an infinity in a query row stays in that row and head, a NaN element of V in its dim of
+    its head; everything else is the oracle's."""
+    from budget_harness import check_attention
+    w = work(head_dim=D, frames=5)
+    h = harness(w, "e4m3", splits=2)
+
+    def kv(f):
+        def rows_of(s, b):
+            k, v = wl.frame_kv(w, s, b, f)
+            v = v.copy()
+            if f == 4:               # (frames 0, 3 and 4 are visible)
+                v[17, 1, 9] = 0x7FC0
+            return k, v
+        return rows_of
+
+    for f in range(w.frames):
+        h.append(f, kv(f))
+    q = h.queries(rows, 3)
+    bad = sorted({0, rows // 2, rows - 1})
+    for i, r in enumerate(bad):
+        q[r, 0, 5] = (0x7FC0, 0x7F80, 0xFF80)[i]         # NaN, inf, -inf
+    h.cache.plan_rows(rows, h.ws, h.st)
+    out, lse = h.attend(0, q)
+    clean = q.copy()
+    clean[bad, 0, 5] = 0
+    assert np.isnan(out[bad, 0]).all() and not np.isfinite(lse[bad, 0]).any()
+    assert np.isnan(out[:, 1, 9]).all()
+    # the rest against an oracle that has neither
+    for key, (k, v) in list(h.patch.items()):
+        h.patch[key] = (k, np.nan_to_num(v))
+    o, l, a, ds, flushed = h.oracle(0, clean, rows)
+    got_o, got_l = out.copy(), lse.copy()
+    got_o[bad, 0], got_l[bad, 0] = o[bad, 0], l[bad, 0]
+    got_o[:, 1, 9] = o[:, 1, 9]
+    check_attention((got_o, got_l), (o, l, a, ds, flushed), "e4m3", f"{rows} rows")
+    assert h.status() == 0
+    h.close()
+
+
 # ---------------------------------------------------------------- workspace
 
 @pytest.mark.parametrize("kind,heads,splits", [("e4m3", 1, 256), ("e4m3", 1, 0), ("e4m3", 16, 256), ("bf16", 2, 32), ("f32", 2, 32)])
