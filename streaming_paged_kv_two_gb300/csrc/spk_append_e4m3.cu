@@ -10,7 +10,7 @@
 // per thread and 8 (D = 64) or 16 threads per (token, head) row: the row's maximum is three or
 // four shuffles, every load and store of a row is contiguous.  Measured: 2.1 us a launch of 262
 // tokens of 16 heads of 64 dims (1.6 MB), 3.9 us of 1005 (6.2 MB, 1.6 TB/s); a host call takes 3 us, the
-// caller's indexing of the rows twice that (24 blocks 75 us with the rows at hand, 250 to 285 without).
+// caller's indexing of the rows twice that (24 blocks 75 us with the rows at hand, 226 to 325 without).
 #include "spk_rope.cuh"
 
 #include <cuda_bf16.h>
